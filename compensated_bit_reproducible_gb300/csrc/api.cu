@@ -639,7 +639,9 @@ cudaError_t by_type16(repro_type t, F f) {
   return t == REPRO_F16 ? f(__half()) : f(__nv_bfloat16());
 }
 
-// Row and column counts that leave a tile's index arithmetic inside 32 bits.
+// Row and column counts that leave the row and column indices of their tiles
+// inside 32 bits.  (The number of tiles is bounded by the workspace, eight bytes
+// a row and half tile or the pieces' g, and checked at the launch.)
 constexpr int64_t XENT_MAX = 1 << 30;
 
 repro_status xent_check(const Mat& h, const Mat& w) {

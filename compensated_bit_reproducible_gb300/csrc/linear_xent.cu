@@ -371,8 +371,8 @@ static cudaError_t run_tiles(const CUtensorMap& a, const CUtensorMap& b, const T
     if (c < 1) return cudaErrorInvalidConfiguration;
     pairs[dev].store(c);
   }
-  const int64_t tiles = (int64_t)sh.mt() * sh.nt() * sh.splits;
-  const int64_t all = pairs[dev].load(), use = tiles < all ? tiles : all;
+  const int64_t tiles = sh.tiles(), all = pairs[dev].load(), use = tiles < all ? tiles : all;
+  if (tiles > TILES_MAX) return cudaErrorInvalidValue;
   return chain.launch(kernel, (unsigned)(2 * use), TG_THREADS, TG_SMEM, a, b, sh, epi, error);
 }
 
@@ -449,7 +449,7 @@ static int split_count(int64_t m, int64_t n, int tn, int64_t k, bool carried) {
 // vocabulary (a tile's weights are read once; 608 us against 618 for 8192 x
 // 32768 x 2048), the products that read g in bands of 8 (305 against 331 us for
 // half of dweight).
-constexpr int BAND = 8, BAND_ALL = 1 << 22;
+constexpr int BAND = 8, BAND_ALL = 0x7fffffff;
 
 // How the gradient of one shape is computed.
 struct XentPlan {

@@ -37,10 +37,10 @@
 #include "elem.cuh"
 #include "launch.h"
 #include "mbarrier.cuh"
+#include "tile_walk.h"
 
 namespace repro {
 
-constexpr int TG_M = 256, TG_N = 256, TG_K = 64;
 constexpr int TG_STAGES = 6, TG_HALF = 128 * TG_K * 2;   // bytes of one block's half of an operand step
 constexpr int TG_STAGE = 2 * TG_HALF;
 constexpr int TG_THREADS = 384, TG_EPI_WARPS = 8;
@@ -118,42 +118,6 @@ __device__ __forceinline__ uint32_t instr_desc(int tn) {
   return 1u << 4 | (BF16 ? 1u << 7 | 1u << 10 : 0u) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u) |
          (uint32_t)(tn >> 3) << 17 | (uint32_t)(TG_M >> 4) << 24;
 }
-
-struct TileShape {
-  int m, n, k;      // rows of A, rows of B, inner dimension
-  int tn, splits;   // columns of a tile, ranges of the inner dimension
-  int bn0, bk0;     // B's first row and first inner index within its tensor map
-  int band;         // order of the tiles, see TileWalk
-  int mt() const { return (m + TG_M - 1) / TG_M; }
-  int nt() const { return (n + tn - 1) / tn; }
-};
-
-// The tiles of a pair, every step-th of them: within a range of the inner
-// dimension, bands of `band` tiles of m; in a band m fastest, then n.  With 8,
-// the tiles in flight form a block of about 8 x 10, which reads fewer different
-// rows of A and B at a time than a column of all m does.
-struct TileWalk {
-  int m, n, split, mt, nt, splits, width;
-  unsigned at, step;
-  __device__ __forceinline__ TileWalk(const TileShape& sh, unsigned first, unsigned stride)
-      : mt((sh.m + TG_M - 1) / TG_M), nt((sh.n + sh.tn - 1) / sh.tn), splits(sh.splits), width(sh.band), at(first),
-        step(stride) {
-    place();
-  }
-  __device__ __forceinline__ void place() {
-    const unsigned flat = (unsigned)mt * (unsigned)nt, s = at / flat, in = at - s * flat;
-    const unsigned band = in / ((unsigned)nt * width), r = in - band * ((unsigned)nt * width);
-    const unsigned high = min((unsigned)width, (unsigned)mt - band * width);
-    split = (int)s;
-    n = (int)(r / high);
-    m = (int)(band * width + r % high);
-  }
-  __device__ __forceinline__ bool more() const { return split < splits; }
-  __device__ __forceinline__ void next() {
-    at += step;
-    place();
-  }
-};
 
 // 32 values of each lane's row, rounded to T and stored as rows of 32 columns
 // from `col`: through `stage`, so that a store covers whole sectors of a row
