@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(256) embed_count(const int64_t* __restrict__ t
   const int t = blockIdx.x * 256 + threadIdx.x;
   const int lane = threadIdx.x & 31;
   int64_t id = t < n ? tok[t] : -1;
-  if (id >= vocab) id = -1;
+  // all that are no row become -1 (below, 32 bits of the token are compared)
+  if (id < 0 || id >= vocab) id = -1;
   const unsigned same = __match_any_sync(0xffffffffu, (int)id);
   const int first = __ffs(same) - 1;
   int base = 0;
