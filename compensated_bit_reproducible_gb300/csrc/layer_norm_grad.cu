@@ -262,7 +262,8 @@ static LnGrad ln_grad_shape(int mode, int64_t rows, int64_t cols, int size) {
     if (!g.stages) g.warps = 0, held = per_sm = 1;
   }
   const int64_t most = 152 * per_sm, want = (rows + 4 * held - 1) / (4 * held);
-  g.blocks = row_blocks(want, most, held, mode);
+  // (the long kernel has no slots that need an even step, and leaves a partial row for each block only if each has a row)
+  g.blocks = g.warps ? row_blocks(want, most, held, mode) : want < most ? want : most;
   return g;
 }
 
