@@ -96,6 +96,22 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """Memory for an output.  It belongs to the stream that the call runs on,
+    as the call's own work is the first to touch it; where that is not the
+    current one, the caller may use and drop it on the current stream too, so
+    it is not handed out again before both are past it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def _ptr(t: torch.Tensor):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else ctypes.c_void_p(0)
 
@@ -171,7 +187,7 @@ def repro_cumsum(x: torch.Tensor, out: torch.Tensor | None = None, K: int = 3, b
     sfx = _sfx(x)
     assert x.is_contiguous()
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream if x.is_cuda else None)
     assert out.dtype == x.dtype and out.is_contiguous() and out.numel() == x.numel()
     _check(getattr(lib(), "repro_cumsum_%s_ex" % sfx)(_ptr(x), _ptr(out), x.numel(), K, _stream(stream),
                                                       _launch(block, 0)), "repro_cumsum_" + sfx)
@@ -183,7 +199,7 @@ def repro_segsum(x: torch.Tensor, axis: int = 1, K: int = 3, out: torch.Tensor |
     assert x.is_cuda and x.dtype == torch.float32 and x.dim() == 2 and x.is_contiguous()
     rows, cols = x.shape
     if out is None:
-        out = torch.empty(rows if axis == 1 else cols, dtype=torch.float32, device=x.device)
+        out = _empty(rows if axis == 1 else cols, torch.float32, x.device, stream)
     _check(lib().repro_segsum_f32(_ptr(x), rows, cols, axis, K, _ptr(out), _stream(stream)), "repro_segsum_f32")
     return out
 
@@ -199,9 +215,9 @@ def stable_var(x: torch.Tensor, axis: int = 1, ddof: int = 0, out=None, mean_out
     ns = rows if axis == 1 else cols
     vdt = {torch.float32: torch.float32, torch.float64: torch.float64, torch.complex64: torch.float32}[x.dtype]
     if out is None:
-        out = torch.empty(ns, dtype=vdt, device=x.device)
+        out = _empty(ns, vdt, x.device, stream)
     if with_mean and mean_out is None:
-        mean_out = torch.empty(ns, dtype=x.dtype, device=x.device)
+        mean_out = _empty(ns, x.dtype, x.device, stream)
     mp = _ptr(mean_out) if with_mean else ctypes.c_void_p(0)
     st = _stream(stream)
     if x.dtype == torch.float32:
@@ -223,7 +239,7 @@ def twoterm_var(x: torch.Tensor, axis: int = 1, ddof: int = 0, out=None, stream=
     assert x.is_cuda and x.dtype == torch.float32 and x.dim() == 2 and x.is_contiguous()
     rows, cols = x.shape
     if out is None:
-        out = torch.empty(rows if axis == 1 else cols, dtype=torch.float32, device=x.device)
+        out = _empty(rows if axis == 1 else cols, torch.float32, x.device, stream)
     _check(lib().twoterm_var_f32(_ptr(x), rows, cols, axis, ddof, _ptr(out), _stream(stream)), "twoterm_var_f32")
     return out
 
@@ -234,7 +250,7 @@ def compare_sum(x: torch.Tensor, mode: str, out: torch.Tensor | None = None, str
     sfx = _sfx(x)
     assert x.is_cuda and x.is_contiguous()
     if out is None:
-        out = torch.empty(1, dtype=x.dtype, device=x.device)
+        out = _empty(1, x.dtype, x.device, stream)
     name = "repro_sum_%s_%s" % (mode, sfx)
     _check(getattr(lib(), name)(_ptr(x), x.numel(), _ptr(out), _stream(stream)), name)
     return out
@@ -262,7 +278,7 @@ def state_new(dtype, K: int = 3, device=None, stream=None) -> torch.Tensor:
     n = state_bytes(K)
     if n == 0:
         raise ReproError(1, "repro_state_bytes")
-    st = torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
+    st = _empty(n, torch.uint8, device or torch.device("cuda", torch.cuda.current_device()), stream)
     state_init(st, dtype, K, stream)
     return st
 
@@ -290,7 +306,7 @@ def state_finalize(state: torch.Tensor, dtype, K: int = 3, out: torch.Tensor | N
     """Correctly rounded value of the state, as a one-element device tensor."""
     sfx = _tsfx(dtype)
     if out is None:
-        out = torch.empty(1, dtype=dtype, device=state.device)
+        out = _empty(1, dtype, state.device, stream)
     _check(getattr(lib(), "repro_state_finalize_" + sfx)(_ptr(state), K, _ptr(out), _stream(stream)),
            "repro_state_finalize_" + sfx)
     return out
@@ -304,7 +320,7 @@ def repro_cumsum_from_state(x: torch.Tensor, state: torch.Tensor, K: int = 3, ou
     sfx = _sfx(x)
     assert x.is_contiguous() and state.dtype == torch.uint8
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream if x.is_cuda else None)
     assert out.dtype == x.dtype and out.is_contiguous() and out.numel() == x.numel()
     _check(getattr(lib(), "repro_cumsum_from_state_" + sfx)(_ptr(x), _ptr(out), x.numel(), K, _ptr(state),
                                                             _stream(stream)), "repro_cumsum_from_state_" + sfx)
@@ -352,10 +368,10 @@ def _vec(t: torch.Tensor | None, dtype, n: int):
     return t.data_ptr()
 
 
-def _out(out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor):
+def _out(out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, stream):
     """An output of `like`'s type: (tensor, pointer, row stride)."""
     if out is None:
-        out = torch.empty(rows, cols, dtype=like.dtype, device=like.device)
+        out = _empty((rows, cols), like.dtype, like.device, stream)
         return out, out.data_ptr(), max(cols, 1)
     p, r, c, ld = _mat(out)
     assert out.dtype == like.dtype and r == rows and c == cols
@@ -368,7 +384,7 @@ def repro_embedding(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1
     token gives a zero row, one past the table a row of NaN."""
     w, vocab, cols, ldw = _mat(weight)
     n = tokens.numel()
-    out, o, ldo = _out(out, n, cols, weight)
+    out, o, ldo = _out(out, n, cols, weight, stream)
     _check(lib().repro_embedding(w, vocab, cols, ldw, _vec(tokens, torch.int64, n), n, scale, _type(weight), o, ldo,
                                  _stream_of(weight, stream)), "repro_embedding")
     return out
@@ -379,7 +395,7 @@ def repro_embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
     """Gradient of repro_embedding to its table: [vocab, cols].  Each element
     is a binned sum (K = 3): its bits do not depend on the tokens' order."""
     y, n, cols, lddy = _mat(dy)
-    out, o, ldo = _out(out, vocab, cols, dy)
+    out, o, ldo = _out(out, vocab, cols, dy, stream)
     _check(lib().repro_embedding_grad(y, lddy, _vec(tokens, torch.int64, n), n, vocab, cols, scale, _type(dy), o, ldo,
                                       _stream_of(dy, stream)), "repro_embedding_grad")
     return out
@@ -390,9 +406,9 @@ def stable_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias:
     """Layer norm of each row of a 2-D tensor: (y, mean, rstd), the last two
     float32.  out may be x itself."""
     p, rows, cols, ldx = _mat(x)
-    out, o, ldo = _out(out, rows, cols, x)
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    out, o, ldo = _out(out, rows, cols, x, stream)
+    mean = _empty(rows, torch.float32, x.device, stream)
+    rstd = _empty(rows, torch.float32, x.device, stream)
     _check(lib().stable_layer_norm(p, rows, cols, ldx, _vec(weight, x.dtype, cols), _vec(bias, x.dtype, cols), eps,
                                    _type(x), o, ldo, mean.data_ptr(), rstd.data_ptr(), _stream_of(x, stream)),
            "stable_layer_norm")
@@ -406,9 +422,9 @@ def stable_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     p, rows, cols, ldx = _mat(x)
     y, dy_rows, dy_cols, lddy = _mat(dy)
     assert dy.dtype == x.dtype and dy_rows == rows and dy_cols == cols
-    out, o, ldo = _out(out, rows, cols, x)
-    dweight = torch.empty(cols, dtype=x.dtype, device=x.device)
-    dbias = torch.empty(cols, dtype=x.dtype, device=x.device)
+    out, o, ldo = _out(out, rows, cols, x, stream)
+    dweight = _empty(cols, x.dtype, x.device, stream)
+    dbias = _empty(cols, x.dtype, x.device, stream)
     _check(lib().stable_layer_norm_grad(y, lddy, p, rows, cols, ldx, _vec(weight, x.dtype, cols),
                                         _vec(mean, torch.float32, rows), _vec(rstd, torch.float32, rows), _type(x), o,
                                         ldo, dweight.data_ptr(), dbias.data_ptr(), _stream_of(x, stream)),
@@ -423,8 +439,8 @@ def stable_linear_xent(h: torch.Tensor, weight: torch.Tensor, labels: torch.Tens
     p, n, cols, ldh = _mat(h)
     w, vocab, w_cols, ldw = _mat(weight)
     assert weight.dtype == h.dtype and w_cols == cols
-    loss = torch.empty(n, dtype=torch.float32, device=h.device)
-    lse = torch.empty(n, dtype=torch.float32, device=h.device)
+    loss = _empty(n, torch.float32, h.device, stream)
+    lse = _empty(n, torch.float32, h.device, stream)
     _check(lib().stable_linear_xent(p, n, cols, ldh, w, vocab, ldw, _vec(labels, torch.int64, n), _type(h),
                                     loss.data_ptr(), lse.data_ptr(), _stream_of(h, stream)), "stable_linear_xent")
     return loss, lse
@@ -438,8 +454,8 @@ def stable_linear_xent_grad(dloss: torch.Tensor, h: torch.Tensor, weight: torch.
     w, vocab, w_cols, ldw = _mat(weight)
     assert weight.dtype == h.dtype and w_cols == cols
     dh, dweight = out if out is not None else (None, None)
-    dh, a, lddh = _out(dh, n, cols, h)
-    dweight, b, lddw = _out(dweight, vocab, cols, h)
+    dh, a, lddh = _out(dh, n, cols, h, stream)
+    dweight, b, lddw = _out(dweight, vocab, cols, h, stream)
     _check(lib().stable_linear_xent_grad(_vec(dloss, torch.float32, n), p, n, cols, ldh, w, vocab, ldw,
                                          _vec(labels, torch.int64, n), _vec(lse, torch.float32, n), _type(h), a, lddh,
                                          b, lddw, _stream_of(h, stream)), "stable_linear_xent_grad")
