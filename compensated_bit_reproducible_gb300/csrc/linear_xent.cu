@@ -120,17 +120,17 @@ struct EpiGrad {
   int64_t ldg;
   int n, width, v0, vocab;   // columns of the piece, its first token
   struct State {
-    float lse2, d;
+    float lse, d;
     int at;   // the label's column in the piece, or -1
   };
   __device__ __forceinline__ void row(int row, State& st) const {
-    st.lse2 = 0.0f;
+    st.lse = 0.0f;
     st.d = 0.0f;
     st.at = -1;
     if (row < n) {
       const int64_t l = label[row];
       if (l >= 0) {
-        st.lse2 = lse[row] * LOG2E;
+        st.lse = lse[row];
         st.d = l < vocab ? __fdiv_rn(dloss[row], scale[0]) * scale[1] : __uint_as_float(0x7fc00000u);
         st.at = l >= v0 && l < v0 + (int64_t)width ? (int)(l - v0) : -1;
       } else {
@@ -140,9 +140,10 @@ struct EpiGrad {
   }
   __device__ __forceinline__ void chunk(int, int col, F2* v, State& st, const Place& at) const {
     if (col >= width) return;
-    const F2 scale = pk2(LOG2E, LOG2E), off = pk2(-st.lse2, -st.lse2), d = pk2(st.d, st.d);
+    // (the difference first, as in the loss: a rounding of lse log2(e) would be an exponent's error past 2^24)
+    const F2 scale = pk2(LOG2E, LOG2E), off = pk2(st.lse, st.lse), d = pk2(st.d, st.d);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = power2(fma2(v[i], scale, off));
+    for (int i = 0; i < 16; ++i) v[i] = power2(mul2(sub2(v[i], off), scale));
     const int hit = st.at - col;
     if (hit >= 0 && hit < 32)
 #pragma unroll

@@ -73,3 +73,16 @@ def test_loss_of_logits_of_any_size(size):
     assert torch.all((lse.double() - top).abs() <= 2.0 ** -22 * top.abs())
     want = top - z.gather(1, t[:, None])[:, 0]
     assert torch.all((loss.double() - want).abs() <= 2.0 ** -22 * (want.abs() + top.abs()) * (want != 0))
+
+
+@pytest.mark.parametrize("size", SIZES)
+def test_gradient_of_logits_of_any_size(size):
+    """One more rounding to 16 bits than the output's own, of terms that do not cancel."""
+    h, w, t = large_logits(size)
+    lse = api.stable_linear_xent(h, w, t)[1]
+    dh, dw = api.stable_linear_xent_grad(torch.ones(3, device=h.device), h, w, t, lse)
+    z = h.double() @ w.double().T
+    g = torch.softmax(z, 1)
+    g[torch.arange(3), t] -= 1.0
+    for got, exact in ((dh, g @ w.double()), (dw, g.T @ h.double())):
+        assert torch.all((got.double() - exact).abs() <= 2.0 ** -7 * exact.abs() + 2.0 ** -12)
