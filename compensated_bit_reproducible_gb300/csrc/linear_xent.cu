@@ -115,7 +115,7 @@ struct EpiGrad {
   const int64_t* label;
   const float* lse;
   const float* dloss;
-  const float* scale;   // [0]: the largest |dloss|, [1]: a power of two
+  const float* scale;   // [0]: the largest finite |dloss|, [1]: a power of two
   T* g;                 // [n][ldg]
   int64_t ldg;
   int n, width, v0, vocab;   // columns of the piece, its first token
@@ -165,7 +165,7 @@ struct EpiOut {
   float* sum;           // [splits][rows][lds] or null
   int64_t lds;          // a multiple of 32
   int add;              // sum holds earlier pieces
-  const float* scale;   // [0]: the largest |dloss|, [2]: the inverse power of two
+  const float* scale;   // [0]: the largest finite |dloss|, [2]: the inverse power of two
   T* out;
   int64_t ldo;
   int rows, cols, wide;   // wide: rows of out are 16-byte aligned
@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(256) xent_join(const float2* __restrict__ part
   loss[row] = id < 0 ? 0.0f : id >= vocab ? nan : (m - zlabel[row]) + above;
 }
 
-// scale[0] = the largest |dloss|, scale[1] = 2^14, scale[2] = 2^-14; 1 where
-// there is nothing to scale by.  The largest itself, not a power of two near it:
+// scale[0] = the largest finite |dloss|, scale[1] = 2^14, scale[2] = 2^-14; 1
+// where there is nothing to scale by.  (An infinity or a NaN stays one at any
+// scale, and the other rows keep theirs.)  The largest itself, not a power of two near it:
 // where all rows have the same dloss (a mean) their quotient is exactly 1, the
 // label's element p - 1 is off by p at most in 16 bits, and no rounding of dloss
 // is shared by all rows.
@@ -248,13 +249,16 @@ __global__ void __launch_bounds__(1024) xent_scale(const float* __restrict__ dlo
   __shared__ unsigned top[32];
   unsigned m = 0;
   for (int i = threadIdx.x; i < n; i += 1024)
-    if (label[i] >= 0) m = max(m, __float_as_uint(fabsf(dloss[i])));
+    if (label[i] >= 0) {
+      const unsigned a = __float_as_uint(fabsf(dloss[i]));
+      if (a < 0x7f800000u) m = max(m, a);
+    }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 32; ++i) m = max(m, top[i]);
-    const bool any = m < 0x7f800000u && m != 0;
+    const bool any = m != 0;
     scale[0] = any ? __uint_as_float(m) : 1.0f;
     scale[1] = any ? 0x1p14f : 1.0f;
     scale[2] = any ? 0x1p-14f : 1.0f;
