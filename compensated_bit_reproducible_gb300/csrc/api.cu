@@ -510,17 +510,21 @@ bool overlap(const Mat& a, const Mat& b) {
 }
 
 // Waits inside the operators' kernels are bounded; one that runs out leaves a mark in
-// pinned host memory (one word for the process), which the next call finds.
+// pinned host memory (one word for the process), which the next call finds.  An
+// allocation that fails (inside a stream capture it may) is tried again by the next call.
 int* tile_error_word() {
-  static int* word = [] {
+  static std::mutex mu;
+  static int* word = nullptr;
+  std::lock_guard<std::mutex> g(mu);
+  if (!word) {
     void* p = nullptr;
     if (cudaHostAlloc(&p, 64, cudaHostAllocPortable | cudaHostAllocMapped) != cudaSuccess) {
       cudaGetLastError();
-      return (int*)nullptr;
+      return nullptr;
     }
     *(int*)p = 0;
-    return (int*)p;
-  }();
+    word = (int*)p;
+  }
   return word;
 }
 

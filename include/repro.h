@@ -294,8 +294,9 @@ int repro_compensated_chunk(void);
       rounded once to the element type at the end;
     - calls are stream-ordered and return once the work is enqueued; workspace
       as for the other calls (the pool, on `stream`); the layer norm and the
-      loss use a word of the stream's control page, so the stream's first such
-      call must come before a capture;
+      loss use a word of the stream's control page and one of pinned host memory,
+      so the process's and the stream's first such call must come before a
+      capture (inside one it fails, and a later call allocates them);
     - waits inside the layer norm's and the loss's kernels (for copies and
       products) are bounded to about two seconds; should one run out, that
       call's outputs are undefined and later calls of these four return
