@@ -535,6 +535,8 @@ repro_status tile_error(cudaStream_t stream, TileError* e) {
   unsigned char* page = nullptr;
   CK(ctl_page(stream, &page));
   e->device = (int*)(page + CTL_TILE_ERROR);
+  e->never = wait_fail_forced();
+  e->limit_ns = e->never ? WAIT_LIMIT_FORCED_NS : WAIT_LIMIT_NS;
   return REPRO_OK;
 }
 
@@ -965,6 +967,10 @@ namespace repro {
 void set_last_cuda(cudaError_t e) { g_last_cuda = (int)e; }
 bool env_fail_forced() {
   const char* force = std::getenv("REPRO_FORCE_ENV_FAIL");
+  return force && force[0] == '1';
+}
+bool wait_fail_forced() {
+  const char* force = std::getenv("REPRO_FORCE_WAIT_FAIL");
   return force && force[0] == '1';
 }
 }  // namespace repro

@@ -97,11 +97,19 @@ constexpr int COMPENSATED_CHUNK = 4096;
 
 // Waits for copies and products inside the model operators' kernels are
 // bounded; one that runs out sets both words: one in device memory, read by
-// later kernels, one in mapped host memory, read by the next call.
+// later kernels, one in mapped host memory, read by the next call.  `never` is
+// 1 to make them run out: the barriers of a kernel's copies then expect one more
+// arrival than there is.
 struct TileError {
   int* device;
   int* host;
+  unsigned limit_ns;
+  unsigned never;
 };
+constexpr unsigned WAIT_LIMIT_NS = 2000000000u, WAIT_LIMIT_FORCED_NS = 1000000u;
+// What a kernel that gave up leaves its copies in flight to land, before it
+// ends and its shared memory is another's.
+constexpr unsigned WAIT_DRAIN_NS = 1000000u;
 // Model operators (embedding.cu, layer_norm.cu), T float, __half or
 // __nv_bfloat16.  ld*: row strides in elements.  Null weights and biases of
 // the layer norm stand for ones and zeros, null gradients are not written.
@@ -143,6 +151,8 @@ cudaError_t launch_linear_xent_grad(const float* dloss, const T* h, int64_t ldh,
 cudaError_t launch_env_probe(unsigned* out, cudaStream_t s);
 // true when REPRO_FORCE_ENV_FAIL=1 asks every environment check to fail
 bool env_fail_forced();
+// true when REPRO_FORCE_WAIT_FAIL=1 asks the model operators' waits to run out
+bool wait_fail_forced();
 
 // The calling host thread's last CUDA error, the one repro_last_cuda_error()
 // returns; every entry point that returns REPRO_ERR_CUDA records its code here.

@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(RowShape<1, WARPS>::BLOCK,
   };
   if (f.t == 0)
     for (int s = 0; s < stages && r + s * step < rows; ++s) fill(s);
-  const int64_t ahead = stages * step;
+  int64_t ahead = stages * step;
   for (; r < rows; r += step) {
-    q.wait();
+    q.wait(ahead);
     const T* p = row_at<T, MODE>(ring + q.s * place, x, ldx, r);
     const T first = p[0];
     const float x0 = to_f32<T>(first);

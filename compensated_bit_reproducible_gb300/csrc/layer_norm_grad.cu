@@ -133,13 +133,13 @@ __global__ void __launch_bounds__(RowShape<1, WARPS>::BLOCK, RowShape<1, WARPS>:
   };
   if (k.t == 0)
     for (int s = 0; s < stages && r + s * step < rows; ++s) fill(s);
-  const int64_t ahead = stages * step;
+  int64_t ahead = stages * step;
   int par = 0;
   float mu = 0.0f, rs = 0.0f;
   if (r < rows) mu = mean[r], rs = rstd[r];
   const T zero = from_f32<T>(0.0f);
   for (; r < rows; r += step, par ^= 1) {
-    q.wait();
+    q.wait(ahead);
     const unsigned char* at = ring + q.s * 2 * place;
     const T *p = row_at<T, MODE>(at, x, ldx, r), *g = row_at<T, MODE>(at + place, dy, lddy, r);
     F2 s0 = 0, s1 = 0;

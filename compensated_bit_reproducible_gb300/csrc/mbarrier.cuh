@@ -12,6 +12,11 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
+__device__ __forceinline__ void pause_ns(unsigned ns) {
+  const uint64_t t0 = now_ns();
+  while (now_ns() - t0 < ns) {
+  }
+}
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }

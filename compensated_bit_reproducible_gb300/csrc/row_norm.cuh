@@ -92,8 +92,13 @@ __device__ __forceinline__ float across(F2 v) {
 
 // A ring of bulk copies into shared memory, one barrier a stage.  Waits are
 // bounded: one that runs out (about two seconds) marks `error` and lets every
-// later one pass, so the block ends with values that mean nothing.
+// later one of its thread pass, so the block ends with values that mean nothing.
+// The thread that fills the ring stops then (the next row to fill is put past the
+// last) and leaves its copies time to land, before the block can end or use the
+// ring for something else.  All of it where a wait runs out: a test in the rows'
+// loop or after it costs the large layer norm 1%.
 constexpr int RING_MAX = 4;
+constexpr int64_t NO_ROW = 1ll << 62;
 struct Ring {
   uint64_t* full;
   int stages, s;
@@ -103,7 +108,7 @@ struct Ring {
   __device__ __forceinline__ Ring(uint64_t* f, int n, TileError e)
       : full(f), stages(n), s(0), phase(0), dead(false), error(e) {}
   __device__ __forceinline__ void init() {
-    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1 + error.never);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __device__ __forceinline__ void expect(int stage, uint32_t bytes) { mbar_expect(smem_u32(&full[stage]), bytes); }
@@ -113,16 +118,19 @@ struct Ring {
         "l"(src), "r"(bytes), "r"(smem_u32(&full[stage]))
         : "memory");
   }
-  __device__ __forceinline__ void wait() {
+  // `ahead`: how far ahead of the row waited for the thread fills.
+  __device__ __forceinline__ void wait(int64_t& ahead) {
     const uint32_t b = smem_u32(&full[s]);
     if (dead || mbar_try(b, phase)) return;
     const uint64_t t0 = now_ns();
     while (!mbar_try(b, phase)) {
-      if (now_ns() - t0 > 2000000000ull) {
+      if (now_ns() - t0 > error.limit_ns) {
         dead = true;
         *(volatile int*)error.device = 1;
         *(volatile int*)error.host = 1;
         __threadfence_system();
+        ahead = NO_ROW;
+        pause_ns(WAIT_DRAIN_NS);
         return;
       }
     }

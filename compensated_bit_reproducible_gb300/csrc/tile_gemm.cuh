@@ -28,7 +28,8 @@
 // Bands of tiles (TileWalk) took half of a weight gradient from 331 to 305 us.
 //
 // Every wait is bounded: after about two seconds it sets both words of TileError and the block
-// winds down (drops its tiles, frees its tensor memory, returns).
+// winds down (drops its tiles, leaves copies and products in flight a
+// millisecond to end, frees its tensor memory, returns).
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -180,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TG_THREADS, 1)
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
     for (int i = 0; i < TG_STAGES; ++i) {
-      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&full[i]), 1 + error.never);
       mbar_init(smem_u32(&empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -211,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TG_THREADS, 1)
       for (int i = 0; i < 64; ++i)
         if (mbar_try(b, parity)) return true;
       if (*(volatile int*)&stop) return false;
-      if (now_ns() - t0 > 2000000000ull) {
+      if (now_ns() - t0 > error.limit_ns) {
         *(volatile int*)&stop = 1;
         *(volatile int*)error.device = 1;
         *(volatile int*)error.host = 1;
@@ -264,12 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TG_THREADS, 1)
       ok = wait(&empty[s], ph ^ 1);
       if (++s == TG_STAGES) s = 0, ph ^= 1;
     }
-    if (!ok) {
-      // copies in flight get a millisecond to land
-      const uint64_t t0 = now_ns();
-      while (now_ns() - t0 < 1000000ull) {
-      }
-    }
+    if (!ok) pause_ns(WAIT_DRAIN_NS);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     const uint32_t idesc = instr_desc<BF16, AMN, BMN>(tn);
     int s = 0, it = 0;
@@ -293,11 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TG_THREADS, 1)
       }
       if (ok) mma_commit_both(smem_u32(&acc_full[buf]));
     }
-    if (!ok) {
-      const uint64_t t0 = now_ns();
-      while (now_ns() - t0 < 1000000ull) {
-      }
-    }
+    if (!ok) pause_ns(WAIT_DRAIN_NS);
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2, runs = tn / 32;
     const int c0 = half ? (runs + 1) / 2 : 0, c1 = half ? runs : (runs + 1) / 2;

@@ -300,7 +300,9 @@ int repro_compensated_chunk(void);
     - waits inside the layer norm's and the loss's kernels (for copies and
       products) are bounded to about two seconds; should one run out, that
       call's outputs are undefined and later calls of these four return
-      REPRO_ERR_DEVICE_TIMEOUT;
+      REPRO_ERR_DEVICE_TIMEOUT (the loss and lse of that call are NaN).  With the
+      environment variable REPRO_FORCE_WAIT_FAIL=1 the waits for copies run out,
+      after a millisecond (a test hook for the failure path);
     - tokens and labels are int64 and read on the device: a negative one is
       padding (no row), one at or past the vocabulary gives NaN;
     - arguments are checked before anything is enqueued: shapes and strides,
