@@ -541,11 +541,14 @@ repro_status tile_error(cudaStream_t stream, TileError* e) {
 }
 
 constexpr int64_t MAX_INT = 0x7fffffff;
+// Columns of an embedding: a warp's last column of a row's last run, up to 1024
+// past the row, is still counted in 32 bits.
+constexpr int64_t EMBED_MAX_COLS = MAX_INT - 4096;
 
 repro_status embedding_impl(const Mat& w, const int64_t* tokens, float scale, repro_type type, const Mat& out,
                             cudaStream_t stream) {
   if (!w.size || !w.shape_ok() || !out.shape_ok()) return REPRO_ERR_INVALID_ARG;
-  if (w.rows > MAX_INT || w.cols > MAX_INT || out.rows > MAX_INT) return REPRO_ERR_CAPACITY;
+  if (w.rows > MAX_INT || w.cols > EMBED_MAX_COLS || out.rows > MAX_INT) return REPRO_ERR_CAPACITY;
   if (out.rows == 0) return REPRO_OK;
   if (!w.ptr_ok() || !out.ptr_ok() || !tokens || !aligned(tokens)) return REPRO_ERR_INVALID_ARG;
   if (overlap(w, out)) return REPRO_ERR_OVERLAP;
@@ -562,7 +565,7 @@ repro_status embedding_impl(const Mat& w, const int64_t* tokens, float scale, re
 repro_status embedding_grad_impl(const Mat& dy, const int64_t* tokens, float scale, repro_type type, const Mat& dw,
                                  cudaStream_t stream) {
   if (!dy.size || !dy.shape_ok() || !dw.shape_ok()) return REPRO_ERR_INVALID_ARG;
-  if (dw.rows > MAX_INT || dy.cols > MAX_INT || dy.rows > MAX_INT) return REPRO_ERR_CAPACITY;
+  if (dw.rows > MAX_INT || dy.cols > EMBED_MAX_COLS || dy.rows > MAX_INT) return REPRO_ERR_CAPACITY;
   if (dw.rows == 0) return REPRO_OK;
   if (!dy.ptr_ok() || !dw.ptr_ok() || (dy.rows && (!tokens || !aligned(tokens)))) return REPRO_ERR_INVALID_ARG;
   if (overlap(dy, dw)) return REPRO_ERR_OVERLAP;

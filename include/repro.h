@@ -306,12 +306,13 @@ int repro_compensated_chunk(void);
     - tokens and labels are int64 and read on the device: a negative one is
       padding (no row), one at or past the vocabulary gives NaN;
     - arguments are checked before anything is enqueued: shapes and strides,
-      then capacity (counts below 2^31), then pointers and alignment, then
+      then capacity (counts below 2^31; less where a call says so), then pointers and alignment, then
       overlap of outputs with inputs (REPRO_ERR_OVERLAP). */
 typedef enum { REPRO_F32 = 0, REPRO_F16 = 1, REPRO_BF16 = 2 } repro_type;
 
 /* out[t] = scale * weight[tokens[t]], t < n; weight is [vocab, cols].  A
-   negative token gives a zero row, one >= vocab a row of NaN. */
+   negative token gives a zero row, one >= vocab a row of NaN.  Here and in the
+   gradient cols is at most 2^31 - 4097. */
 repro_status repro_embedding(const void* weight, int64_t vocab, int64_t cols, int64_t ldw, const int64_t* tokens,
                              int64_t n, float scale, repro_type type, void* out, int64_t ldo, cudaStream_t stream);
 /* dweight[v] = scale * sum of dy[t] over {t : tokens[t] = v}, all vocab rows
@@ -329,7 +330,8 @@ repro_status repro_embedding_grad(const void* dy, int64_t lddy, const int64_t* t
    the variance (ddof 0) by the steps of stable_var_f32: shift by the row's
    first element, centring, two-term correction; sums are plain float32 on a
    fixed topology.  weight and bias ([cols], or null for ones / zeros) have
-   x's type; mean and rstd are float32 [rows].  y may be x.  eps >= 0.  The
+   x's type; mean and rstd are float32 [rows].  y may be x.  eps >= 0, cols at
+   most 2^24 (the gradient's too).  The
    bits depend on values, shape, type and alignment, never on scheduling. */
 repro_status stable_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, const void* weight,
                                const void* bias, float eps, repro_type type, void* y, int64_t ldy, float* mean,
