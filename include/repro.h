@@ -307,7 +307,8 @@ int repro_compensated_chunk(void);
       padding (no row), one at or past the vocabulary gives NaN;
     - arguments are checked before anything is enqueued: shapes and strides,
       then capacity (counts below 2^31; less where a call says so), then pointers and alignment, then
-      overlap of outputs with inputs (REPRO_ERR_OVERLAP). */
+      overlap of outputs with inputs (REPRO_ERR_OVERLAP; column slices of one
+      buffer that share no element do not overlap). */
 typedef enum { REPRO_F32 = 0, REPRO_F16 = 1, REPRO_BF16 = 2 } repro_type;
 
 /* out[t] = scale * weight[tokens[t]], t < n; weight is [vocab, cols].  A
@@ -350,8 +351,8 @@ repro_status stable_layer_norm_grad(const void* dy, int64_t lddy, const void* x,
    h is [n, cols], weight [vocab, cols], both REPRO_F16 or both REPRO_BF16
    (REPRO_F32 is REPRO_ERR_INVALID_ARG: the products run on the tensor cores
    with float32 accumulators).  A negative label gives loss 0, one >= vocab
-   loss NaN; lse is written for every row.  The logits are never kept: the
-   workspace is 8 n bytes per 16 to 128 columns of the vocabulary (128 but for
+   loss NaN; lse is written for every row.  n, vocab and cols are at most 2^30.
+   The logits are never kept: the workspace is 8 n bytes per 16 to 128 columns of the vocabulary (128 but for
    few rows), plus copies of operands whose base or row stride is not a multiple
    of 16 bytes. */
 repro_status stable_linear_xent(const void* h, int64_t n, int64_t cols, int64_t ldh, const void* weight,
