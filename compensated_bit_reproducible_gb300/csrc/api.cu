@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <cuda_bf16.h>
@@ -517,6 +518,13 @@ bool overlap(const Mat& a, const Mat& b) {
   return after < (uintptr_t)a.cols * a.size || after + (uintptr_t)b.cols * b.size > step;
 }
 
+Mat vec(const void* p, int64_t n, size_t size) { return Mat{p, n ? 1 : 0, n ? n : 1, n ? n : 1, size}; }
+bool overlap(const Mat& out, std::initializer_list<Mat> in) {
+  for (const Mat& m : in)
+    if (overlap(out, m)) return true;
+  return false;
+}
+
 // Waits inside the operators' kernels are bounded; one that runs out leaves a mark in
 // pinned host memory (one word for the process), which the next call finds.  An
 // allocation that fails (inside a stream capture it may) is tried again by the next call.
@@ -559,7 +567,7 @@ repro_status embedding_impl(const Mat& w, const int64_t* tokens, float scale, re
   if (w.rows > MAX_INT || w.cols > EMBED_MAX_COLS || out.rows > MAX_INT) return REPRO_ERR_CAPACITY;
   if (out.rows == 0) return REPRO_OK;
   if (!w.ptr_ok() || !out.ptr_ok() || !tokens || !aligned(tokens)) return REPRO_ERR_INVALID_ARG;
-  if (overlap(w, out)) return REPRO_ERR_OVERLAP;
+  if (overlap(out, {w, vec(tokens, out.rows, 8)})) return REPRO_ERR_OVERLAP;
   repro_status st = validate_env(stream);
   if (st != REPRO_OK) return st;
   CK(by_type(type, [&](auto t) {
@@ -576,7 +584,7 @@ repro_status embedding_grad_impl(const Mat& dy, const int64_t* tokens, float sca
   if (dw.rows > MAX_INT || dy.cols > EMBED_MAX_COLS || dy.rows > MAX_INT) return REPRO_ERR_CAPACITY;
   if (dw.rows == 0) return REPRO_OK;
   if (!dy.ptr_ok() || !dw.ptr_ok() || (dy.rows && (!tokens || !aligned(tokens)))) return REPRO_ERR_INVALID_ARG;
-  if (overlap(dy, dw)) return REPRO_ERR_OVERLAP;
+  if (overlap(dw, {dy, vec(tokens, dy.rows, 8)})) return REPRO_ERR_OVERLAP;
   repro_status st = validate_env(stream);
   if (st != REPRO_OK) return st;
   Scratch ws;
@@ -606,7 +614,10 @@ repro_status layer_norm_impl(const Mat& x, const void* w, const void* b, float e
   if (!x.ptr_ok() || !y.ptr_ok() || !vec_ok(w, x.size) || !vec_ok(b, x.size) || !mean || !rstd || !aligned(mean) ||
       !aligned(rstd))
     return REPRO_ERR_INVALID_ARG;
-  if (overlap(x, y) && !(x.p == y.p && x.ld == y.ld)) return REPRO_ERR_OVERLAP;
+  const Mat wv = vec(w, x.cols, x.size), bv = vec(b, x.cols, x.size);
+  if ((overlap(x, y) && !(x.p == y.p && x.ld == y.ld)) || overlap(y, {wv, bv}) ||
+      overlap(vec(mean, x.rows, 4), {x, wv, bv}) || overlap(vec(rstd, x.rows, 4), {x, wv, bv}))
+    return REPRO_ERR_OVERLAP;
   repro_status st = validate_env(stream);
   if (st != REPRO_OK) return st;
   TileError error;
@@ -626,7 +637,10 @@ repro_status layer_norm_grad_impl(const Mat& dy, const Mat& x, const void* w, co
   if (!x.ptr_ok() || !dy.ptr_ok() || !dx.ptr_ok() || !vec_ok(w, x.size) || !vec_ok(dw, x.size) ||
       !vec_ok(db, x.size) || (x.rows && (!mean || !rstd)) || !aligned(mean) || !aligned(rstd))
     return REPRO_ERR_INVALID_ARG;
-  if (overlap(dx, x) || (overlap(dx, dy) && !(dx.p == dy.p && dx.ld == dy.ld))) return REPRO_ERR_OVERLAP;
+  const Mat wv = vec(w, x.cols, x.size), mv = vec(mean, x.rows, 4), rv = vec(rstd, x.rows, 4);
+  if ((overlap(dx, dy) && !(dx.p == dy.p && dx.ld == dy.ld)) || overlap(dx, {x, wv, mv, rv}) ||
+      overlap(vec(dw, x.cols, x.size), {dy, x, wv, mv, rv}) || overlap(vec(db, x.cols, x.size), {dy, x, wv, mv, rv}))
+    return REPRO_ERR_OVERLAP;
   repro_status st = validate_env(stream);
   if (st != REPRO_OK) return st;
   if (x.rows == 0) {   // empty sums
@@ -674,6 +688,8 @@ repro_status linear_xent_impl(const Mat& h, const Mat& w, const int64_t* labels,
   if (h.rows == 0) return REPRO_OK;
   if (!h.ptr_ok() || !w.ptr_ok() || !labels || !aligned(labels) || !loss || !aligned(loss) || !lse || !aligned(lse))
     return REPRO_ERR_INVALID_ARG;
+  const Mat lv = vec(labels, h.rows, 8);
+  if (overlap(vec(loss, h.rows, 4), {h, w, lv}) || overlap(vec(lse, h.rows, 4), {h, w, lv})) return REPRO_ERR_OVERLAP;
   if ((st = validate_env(stream)) != REPRO_OK) return st;
   TileError error;
   if ((st = tile_error(stream, &error)) != REPRO_OK) return st;
@@ -701,8 +717,8 @@ repro_status linear_xent_grad_impl(const float* dloss, const Mat& h, const Mat& 
   if (h.rows && (!h.ptr_ok() || !w.ptr_ok() || !dh.ptr_ok() || !labels || !aligned(labels) || !lse || !aligned(lse) ||
                  !dloss || !aligned(dloss)))
     return REPRO_ERR_INVALID_ARG;
-  if (overlap(dh, h) || overlap(dh, w) || overlap(dw, h) || overlap(dw, w) || overlap(dh, dw))
-    return REPRO_ERR_OVERLAP;
+  const Mat dv = vec(dloss, h.rows, 4), lv = vec(labels, h.rows, 8), sv = vec(lse, h.rows, 4);
+  if (overlap(dh, {h, w, dw, dv, lv, sv}) || overlap(dw, {h, w, dv, lv, sv})) return REPRO_ERR_OVERLAP;
   if ((st = validate_env(stream)) != REPRO_OK) return st;
   if (h.rows == 0) {   // empty sums
     CK(cudaMemset2DAsync((void*)dw.p, dw.ld * dw.size, 0, dw.cols * dw.size, dw.rows, stream));

@@ -4,8 +4,8 @@ import ctypes
 
 import pytest
 
-from tests.test_model_ops_refusals import (ENV, OVERLAP, A, B, C, L, embedding, embedding_grad, layer_norm,  # noqa: F401
-                                           layer_norm_grad, xent_grad)
+from tests.test_model_ops_refusals import (ENV, OVERLAP, A, B, C, D, E, L, embedding, embedding_grad, layer_norm,  # noqa: F401
+                                           layer_norm_grad, xent, xent_grad)
 
 P = ctypes.c_void_p
 
@@ -57,3 +57,29 @@ SHARED = [
 @pytest.mark.parametrize("call,change", SHARED)
 def test_shared_elements(L, call, change):
     assert call(L, **change) == OVERLAP
+
+
+# the same of vectors: tokens and labels (B, C, D below), weights, statistics; one element in common
+VECTORS = [
+    (embedding, dict(out=at(B, 3, 8))), (embedding_grad, dict(dw=at(B, 3, 8))),
+    (layer_norm, dict(y=at(B, 7))), (layer_norm, dict(y=at(C, 7))), (layer_norm, dict(mean=at(A, 30))),
+    (layer_norm, dict(mean=at(B, 6))), (layer_norm, dict(rstd=at(C, 6))), (layer_norm, dict(rstd=A)),
+    (layer_norm_grad, dict(dx=at(C, 7))), (layer_norm_grad, dict(dx=at(D, 3, 4))), (layer_norm_grad, dict(dx=E)),
+    (layer_norm_grad, dict(dw=at(A, 31))), (layer_norm_grad, dict(dw=C)), (layer_norm_grad, dict(db=at(B, 31))),
+    (layer_norm_grad, dict(db=at(D, 3, 4))), (layer_norm_grad, dict(dw=E)),
+    (xent, dict(loss=A)), (xent, dict(loss=at(B, 78))), (xent, dict(lse=at(C, 3, 8))), (xent, dict(lse=A)),
+    (xent_grad, dict(dh=at(A, 3, 4))), (xent_grad, dict(dh=D)), (xent_grad, dict(dw=E)), (xent_grad, dict(dw=at(D, 3, 8))),
+]
+
+
+@pytest.mark.parametrize("call,change", VECTORS)
+def test_vectors_in_an_output(L, call, change):
+    assert call(L, **change) == OVERLAP
+
+
+@pytest.mark.parametrize("call,change", [
+    (embedding, dict(out=at(B, 4, 8))), (layer_norm, dict(y=A)), (layer_norm, dict(y=at(B, 8))), (layer_norm, dict(mean=at(A, 32))),
+    (layer_norm, dict(w=None, b=None)), (layer_norm_grad, dict(dx=A)), (layer_norm_grad, dict(dw=None, db=None)),
+    (layer_norm_grad, dict(dx=at(D, 4, 4))), (xent, dict(loss=at(C, 4, 8))), (xent_grad, dict(dh=at(E, 4, 4)))])
+def test_vectors_beside_an_output(L, call, change):
+    assert call(L, **change) == ENV
