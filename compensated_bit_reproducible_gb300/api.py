@@ -8,6 +8,7 @@ PyTorch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -96,18 +97,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
-    """Memory for an output.  It belongs to the stream that the call runs on,
-    as the call's own work is the first to touch it; where that is not the
-    current one, the caller may use and drop it on the current stream too, so
-    it is not handed out again before both are past it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty_on(stream):
+    """torch.empty for the outputs of a call on `stream`.  They belong to that
+    stream, as the call's own work is the first to touch them; where it is not
+    the current one, the caller may use and drop them on the current stream
+    too, so they are not handed out again before both are past them."""
+    return torch.empty if stream is None else functools.partial(_empty_of, stream)
+
+
+def _empty_of(stream, *shape, dtype, device):
     current = torch.cuda.current_stream(device)
     if stream == current:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty(*shape, dtype=dtype, device=device)
     out.record_stream(current)
     return out
 
@@ -187,7 +190,7 @@ def repro_cumsum(x: torch.Tensor, out: torch.Tensor | None = None, K: int = 3, b
     sfx = _sfx(x)
     assert x.is_contiguous()
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream if x.is_cuda else None)
+        out = _empty_on(stream if x.is_cuda else None)(x.shape, dtype=x.dtype, device=x.device)
     assert out.dtype == x.dtype and out.is_contiguous() and out.numel() == x.numel()
     _check(getattr(lib(), "repro_cumsum_%s_ex" % sfx)(_ptr(x), _ptr(out), x.numel(), K, _stream(stream),
                                                       _launch(block, 0)), "repro_cumsum_" + sfx)
@@ -199,7 +202,7 @@ def repro_segsum(x: torch.Tensor, axis: int = 1, K: int = 3, out: torch.Tensor |
     assert x.is_cuda and x.dtype == torch.float32 and x.dim() == 2 and x.is_contiguous()
     rows, cols = x.shape
     if out is None:
-        out = _empty(rows if axis == 1 else cols, torch.float32, x.device, stream)
+        out = _empty_on(stream)(rows if axis == 1 else cols, dtype=torch.float32, device=x.device)
     _check(lib().repro_segsum_f32(_ptr(x), rows, cols, axis, K, _ptr(out), _stream(stream)), "repro_segsum_f32")
     return out
 
@@ -215,9 +218,9 @@ def stable_var(x: torch.Tensor, axis: int = 1, ddof: int = 0, out=None, mean_out
     ns = rows if axis == 1 else cols
     vdt = {torch.float32: torch.float32, torch.float64: torch.float64, torch.complex64: torch.float32}[x.dtype]
     if out is None:
-        out = _empty(ns, vdt, x.device, stream)
+        out = _empty_on(stream)(ns, dtype=vdt, device=x.device)
     if with_mean and mean_out is None:
-        mean_out = _empty(ns, x.dtype, x.device, stream)
+        mean_out = _empty_on(stream)(ns, dtype=x.dtype, device=x.device)
     mp = _ptr(mean_out) if with_mean else ctypes.c_void_p(0)
     st = _stream(stream)
     if x.dtype == torch.float32:
@@ -239,7 +242,7 @@ def twoterm_var(x: torch.Tensor, axis: int = 1, ddof: int = 0, out=None, stream=
     assert x.is_cuda and x.dtype == torch.float32 and x.dim() == 2 and x.is_contiguous()
     rows, cols = x.shape
     if out is None:
-        out = _empty(rows if axis == 1 else cols, torch.float32, x.device, stream)
+        out = _empty_on(stream)(rows if axis == 1 else cols, dtype=torch.float32, device=x.device)
     _check(lib().twoterm_var_f32(_ptr(x), rows, cols, axis, ddof, _ptr(out), _stream(stream)), "twoterm_var_f32")
     return out
 
@@ -250,7 +253,7 @@ def compare_sum(x: torch.Tensor, mode: str, out: torch.Tensor | None = None, str
     sfx = _sfx(x)
     assert x.is_cuda and x.is_contiguous()
     if out is None:
-        out = _empty(1, x.dtype, x.device, stream)
+        out = _empty_on(stream)(1, dtype=x.dtype, device=x.device)
     name = "repro_sum_%s_%s" % (mode, sfx)
     _check(getattr(lib(), name)(_ptr(x), x.numel(), _ptr(out), _stream(stream)), name)
     return out
@@ -278,7 +281,7 @@ def state_new(dtype, K: int = 3, device=None, stream=None) -> torch.Tensor:
     n = state_bytes(K)
     if n == 0:
         raise ReproError(1, "repro_state_bytes")
-    st = _empty(n, torch.uint8, device or torch.device("cuda", torch.cuda.current_device()), stream)
+    st = _empty_on(stream)(n, dtype=torch.uint8, device=device or torch.device("cuda", torch.cuda.current_device()))
     state_init(st, dtype, K, stream)
     return st
 
@@ -306,7 +309,7 @@ def state_finalize(state: torch.Tensor, dtype, K: int = 3, out: torch.Tensor | N
     """Correctly rounded value of the state, as a one-element device tensor."""
     sfx = _tsfx(dtype)
     if out is None:
-        out = _empty(1, dtype, state.device, stream)
+        out = _empty_on(stream)(1, dtype=dtype, device=state.device)
     _check(getattr(lib(), "repro_state_finalize_" + sfx)(_ptr(state), K, _ptr(out), _stream(stream)),
            "repro_state_finalize_" + sfx)
     return out
@@ -320,7 +323,7 @@ def repro_cumsum_from_state(x: torch.Tensor, state: torch.Tensor, K: int = 3, ou
     sfx = _sfx(x)
     assert x.is_contiguous() and state.dtype == torch.uint8
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream if x.is_cuda else None)
+        out = _empty_on(stream if x.is_cuda else None)(x.shape, dtype=x.dtype, device=x.device)
     assert out.dtype == x.dtype and out.is_contiguous() and out.numel() == x.numel()
     _check(getattr(lib(), "repro_cumsum_from_state_" + sfx)(_ptr(x), _ptr(out), x.numel(), K, _ptr(state),
                                                             _stream(stream)), "repro_cumsum_from_state_" + sfx)
@@ -341,39 +344,43 @@ def _type(t: torch.Tensor) -> int:
 # These calls are short enough for the lookup of the current stream to show:
 # the raw handle skips torch.cuda.Stream's construction (3 us of a 10 us call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream_of(t: torch.Tensor, stream) -> int:
+# Every tensor of a call is on one device, the first one's (`dev`), and that is
+# the current one, where the C ABI launches.
+def _stream_on(dev: int, stream) -> int:
+    assert dev == _device()
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _mat(t: torch.Tensor):
+def _mat(t: torch.Tensor, dev: int):
     """(pointer, rows, columns, row stride) of a 2-D tensor whose rows are
     contiguous.  A single row or none has no stride of its own."""
-    assert t.is_cuda and t.dim() == 2
+    assert t.get_device() == dev >= 0 and t.dim() == 2
     rows, cols = t.shape
     ld, one = t.stride()
     assert one == 1 or rows * cols <= 1 or cols <= 1
     return t.data_ptr(), rows, cols, (ld if rows > 1 else max(ld, cols))
 
 
-def _vec(t: torch.Tensor | None, dtype, n: int):
+def _vec(t: torch.Tensor | None, dtype, n: int, dev: int):
     if t is None:
         return None
-    assert t.is_cuda and t.dtype == dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous()
+    assert t.get_device() == dev and t.dtype == dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous()
     return t.data_ptr()
 
 
-def _out(out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, stream):
+def _out(out: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, dev: int, stream):
     """An output of `like`'s type: (tensor, pointer, row stride)."""
     if out is None:
-        out = _empty((rows, cols), like.dtype, like.device, stream)
+        out = _empty_on(stream)(rows, cols, dtype=like.dtype, device=like.device)
         return out, out.data_ptr(), max(cols, 1)
-    p, r, c, ld = _mat(out)
+    p, r, c, ld = _mat(out, dev)
     assert out.dtype == like.dtype and r == rows and c == cols
     return out, p, ld
 
@@ -382,11 +389,12 @@ def repro_embedding(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1
                     stream=None) -> torch.Tensor:
     """scale * weight[tokens]: [n, cols] for int64 tokens [n]; a negative
     token gives a zero row, one past the table a row of NaN."""
-    w, vocab, cols, ldw = _mat(weight)
+    dev = weight.get_device()
+    w, vocab, cols, ldw = _mat(weight, dev)
     n = tokens.numel()
-    out, o, ldo = _out(out, n, cols, weight, stream)
-    _check(lib().repro_embedding(w, vocab, cols, ldw, _vec(tokens, torch.int64, n), n, scale, _type(weight), o, ldo,
-                                 _stream_of(weight, stream)), "repro_embedding")
+    out, o, ldo = _out(out, n, cols, weight, dev, stream)
+    _check(lib().repro_embedding(w, vocab, cols, ldw, _vec(tokens, torch.int64, n, dev), n, scale, _type(weight), o,
+                                 ldo, _stream_on(dev, stream)), "repro_embedding")
     return out
 
 
@@ -394,10 +402,11 @@ def repro_embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, vocab: int, sca
                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Gradient of repro_embedding to its table: [vocab, cols].  Each element
     is a binned sum (K = 3): its bits do not depend on the tokens' order."""
-    y, n, cols, lddy = _mat(dy)
-    out, o, ldo = _out(out, vocab, cols, dy, stream)
-    _check(lib().repro_embedding_grad(y, lddy, _vec(tokens, torch.int64, n), n, vocab, cols, scale, _type(dy), o, ldo,
-                                      _stream_of(dy, stream)), "repro_embedding_grad")
+    dev = dy.get_device()
+    y, n, cols, lddy = _mat(dy, dev)
+    out, o, ldo = _out(out, vocab, cols, dy, dev, stream)
+    _check(lib().repro_embedding_grad(y, lddy, _vec(tokens, torch.int64, n, dev), n, vocab, cols, scale, _type(dy), o,
+                                      ldo, _stream_on(dev, stream)), "repro_embedding_grad")
     return out
 
 
@@ -405,13 +414,15 @@ def stable_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias:
                       eps: float = 1e-5, out: torch.Tensor | None = None, stream=None):
     """Layer norm of each row of a 2-D tensor: (y, mean, rstd), the last two
     float32.  out may be x itself."""
-    p, rows, cols, ldx = _mat(x)
-    out, o, ldo = _out(out, rows, cols, x, stream)
-    mean = _empty(rows, torch.float32, x.device, stream)
-    rstd = _empty(rows, torch.float32, x.device, stream)
-    _check(lib().stable_layer_norm(p, rows, cols, ldx, _vec(weight, x.dtype, cols), _vec(bias, x.dtype, cols), eps,
-                                   _type(x), o, ldo, mean.data_ptr(), rstd.data_ptr(), _stream_of(x, stream)),
-           "stable_layer_norm")
+    dev = x.get_device()
+    p, rows, cols, ldx = _mat(x, dev)
+    out, o, ldo = _out(out, rows, cols, x, dev, stream)
+    empty = _empty_on(stream)
+    mean = empty(rows, dtype=torch.float32, device=x.device)
+    rstd = empty(rows, dtype=torch.float32, device=x.device)
+    _check(lib().stable_layer_norm(p, rows, cols, ldx, _vec(weight, x.dtype, cols, dev),
+                                   _vec(bias, x.dtype, cols, dev), eps, _type(x), o, ldo, mean.data_ptr(),
+                                   rstd.data_ptr(), _stream_on(dev, stream)), "stable_layer_norm")
     return out, mean, rstd
 
 
@@ -419,16 +430,18 @@ def stable_layer_norm_grad(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tens
                            rstd: torch.Tensor, out: torch.Tensor | None = None, stream=None):
     """Gradient of stable_layer_norm: (dx, dweight, dbias).  out (for dx) may
     be dy itself."""
-    p, rows, cols, ldx = _mat(x)
-    y, dy_rows, dy_cols, lddy = _mat(dy)
+    dev = x.get_device()
+    p, rows, cols, ldx = _mat(x, dev)
+    y, dy_rows, dy_cols, lddy = _mat(dy, dev)
     assert dy.dtype == x.dtype and dy_rows == rows and dy_cols == cols
-    out, o, ldo = _out(out, rows, cols, x, stream)
-    dweight = _empty(cols, x.dtype, x.device, stream)
-    dbias = _empty(cols, x.dtype, x.device, stream)
-    _check(lib().stable_layer_norm_grad(y, lddy, p, rows, cols, ldx, _vec(weight, x.dtype, cols),
-                                        _vec(mean, torch.float32, rows), _vec(rstd, torch.float32, rows), _type(x), o,
-                                        ldo, dweight.data_ptr(), dbias.data_ptr(), _stream_of(x, stream)),
-           "stable_layer_norm_grad")
+    out, o, ldo = _out(out, rows, cols, x, dev, stream)
+    empty = _empty_on(stream)
+    dweight = empty(cols, dtype=x.dtype, device=x.device)
+    dbias = empty(cols, dtype=x.dtype, device=x.device)
+    _check(lib().stable_layer_norm_grad(y, lddy, p, rows, cols, ldx, _vec(weight, x.dtype, cols, dev),
+                                        _vec(mean, torch.float32, rows, dev), _vec(rstd, torch.float32, rows, dev),
+                                        _type(x), o, ldo, dweight.data_ptr(), dbias.data_ptr(),
+                                        _stream_on(dev, stream)), "stable_layer_norm_grad")
     return out, dweight, dbias
 
 
@@ -436,13 +449,15 @@ def stable_linear_xent(h: torch.Tensor, weight: torch.Tensor, labels: torch.Tens
     """Softmax cross entropy of h @ weight.T (float16 or bfloat16) against
     int64 labels, without keeping the logits: (loss, lse), float32 per row.  A
     negative label gives loss 0."""
-    p, n, cols, ldh = _mat(h)
-    w, vocab, w_cols, ldw = _mat(weight)
+    dev = h.get_device()
+    p, n, cols, ldh = _mat(h, dev)
+    w, vocab, w_cols, ldw = _mat(weight, dev)
     assert weight.dtype == h.dtype and w_cols == cols
-    loss = _empty(n, torch.float32, h.device, stream)
-    lse = _empty(n, torch.float32, h.device, stream)
-    _check(lib().stable_linear_xent(p, n, cols, ldh, w, vocab, ldw, _vec(labels, torch.int64, n), _type(h),
-                                    loss.data_ptr(), lse.data_ptr(), _stream_of(h, stream)), "stable_linear_xent")
+    empty = _empty_on(stream)
+    loss = empty(n, dtype=torch.float32, device=h.device)
+    lse = empty(n, dtype=torch.float32, device=h.device)
+    _check(lib().stable_linear_xent(p, n, cols, ldh, w, vocab, ldw, _vec(labels, torch.int64, n, dev), _type(h),
+                                    loss.data_ptr(), lse.data_ptr(), _stream_on(dev, stream)), "stable_linear_xent")
     return loss, lse
 
 
@@ -450,13 +465,15 @@ def stable_linear_xent_grad(dloss: torch.Tensor, h: torch.Tensor, weight: torch.
                             lse: torch.Tensor, out=None, stream=None):
     """Gradient of stable_linear_xent for dloss (float32 per row): (dh,
     dweight).  out: a pair of tensors to write them to."""
-    p, n, cols, ldh = _mat(h)
-    w, vocab, w_cols, ldw = _mat(weight)
+    dev = h.get_device()
+    p, n, cols, ldh = _mat(h, dev)
+    w, vocab, w_cols, ldw = _mat(weight, dev)
     assert weight.dtype == h.dtype and w_cols == cols
     dh, dweight = out if out is not None else (None, None)
-    dh, a, lddh = _out(dh, n, cols, h, stream)
-    dweight, b, lddw = _out(dweight, vocab, cols, h, stream)
-    _check(lib().stable_linear_xent_grad(_vec(dloss, torch.float32, n), p, n, cols, ldh, w, vocab, ldw,
-                                         _vec(labels, torch.int64, n), _vec(lse, torch.float32, n), _type(h), a, lddh,
-                                         b, lddw, _stream_of(h, stream)), "stable_linear_xent_grad")
+    dh, a, lddh = _out(dh, n, cols, h, dev, stream)
+    dweight, b, lddw = _out(dweight, vocab, cols, h, dev, stream)
+    _check(lib().stable_linear_xent_grad(_vec(dloss, torch.float32, n, dev), p, n, cols, ldh, w, vocab, ldw,
+                                         _vec(labels, torch.int64, n, dev), _vec(lse, torch.float32, n, dev),
+                                         _type(h), a, lddh, b, lddw, _stream_on(dev, stream)),
+           "stable_linear_xent_grad")
     return dh, dweight

@@ -4,6 +4,7 @@
 // before the pointer is inspected).  Temporary memory comes from the
 // stream-ordered allocator on the caller's stream.
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -530,18 +531,19 @@ bool overlap(const Mat& out, std::initializer_list<Mat> in) {
 // allocation that fails (inside a stream capture it may) is tried again by the next call.
 int* tile_error_word() {
   static std::mutex mu;
-  static int* word = nullptr;
+  static std::atomic<int*> word{nullptr};
+  if (int* w = word.load()) return w;
   std::lock_guard<std::mutex> g(mu);
-  if (!word) {
+  if (!word.load()) {
     void* p = nullptr;
     if (cudaHostAlloc(&p, 64, cudaHostAllocPortable | cudaHostAllocMapped) != cudaSuccess) {
       cudaGetLastError();
       return nullptr;
     }
     *(int*)p = 0;
-    word = (int*)p;
+    word.store((int*)p);
   }
-  return word;
+  return word.load();
 }
 
 repro_status tile_error(cudaStream_t stream, TileError* e) {
