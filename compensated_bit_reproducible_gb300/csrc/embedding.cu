@@ -775,7 +775,9 @@ __global__ void __launch_bounds__(128)
 // of table rows and some of their column tiles, finds its positions among all
 // tokens, and lists them by row in shared memory (in any order).  509 x 769
 // float32 over 10007 tokens: 12 us, the zeros (31 MB) among them; with
-// the sorted path's six launches 22 us.
+// the sorted path's six launches 21 us.  1024 positions: 15 and 28; 1024 x 2048
+// over 50000 tokens 77 and 88.  (Where one token holds all 1024, the sorted path
+// is the faster from 1024 columns on: 46 against 55 us.)
 constexpr int SMALL_N = 1024, SMALL_ROWS = 512;
 // A row of up to ALONE positions is summed by one warp per tile, a longer one
 // by all eight, each an eighth of its positions.
@@ -873,9 +875,16 @@ __global__ void __launch_bounds__(RED_T, 2)
 template <typename T, int V, int REP>
 static cudaError_t embed_small_run(const T* dy, int64_t lddy, const int64_t* tok, int64_t n, int64_t vocab,
                                    int64_t cols, float scale, T* dw, int64_t lddw, int tiles, int sms, cudaStream_t s) {
-  // Two blocks per SM, as ranges of rows by groups of tiles.  One token may hold every position, and its block then
-  // sums them alone: more groups bound that (509 x 769, common tokens: 10.5 us with 2 groups, 12 with 4, 18 with 8).
-  const int most = n <= SMALL_N / 2 ? 4 : 8, groups = tiles < most ? tiles : most, group = (tiles + groups - 1) / groups, gy = (tiles + group - 1) / group;
+  // Two blocks per SM, as ranges of rows by groups of tiles.  One token may hold many positions, and its block then
+  // sums them alone: more groups bound that, and make every block look for its positions among more rows.  On the
+  // device, over 10007 x 769, tokens by 1 / rank (a mean of ten draws), 4 groups and 8 in us:
+  //               128            256            384            509            1024 positions
+  //   float32      8.2 and 9.4    9.7 and 10.4  11.7 and 11.4  12.2 and 12.0  16.3 and 14.4
+  //   bfloat16     6.7 and 7.3    8.3 and 8.2   10.2 and 9.3   10.8 and 9.9   14.9 and 12.4
+  // One token for all: 256 positions 21 and 12, 1024 58 and 24; all tokens alike likely: 8.0 and 10.2, 11.6 and 15.6
+  // (float32).  2 groups take 1 to 4 us more from 384 positions on; 16 are no faster before 2048 columns.
+  const int most = n <= SMALL_N / 4 ? 4 : 8, groups = tiles < most ? tiles : most;
+  const int group = (tiles + groups - 1) / groups, gy = (tiles + group - 1) / group;
   const int64_t want = (2 * (int64_t)sms + gy - 1) / gy, range = (vocab + want - 1) / want;
   const dim3 grid((unsigned)((vocab + range - 1) / range), (unsigned)gy);
   embed_small<T, V, REP><<<grid, RED_T, 0, s>>>(dy, lddy, tok, (int)n, vocab, cols, scale, dw, lddw, range, tiles,
