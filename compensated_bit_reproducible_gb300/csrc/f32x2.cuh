@@ -34,8 +34,9 @@ __device__ __forceinline__ F2 sub2(F2 a, F2 b) {
   return r;
 }
 
-// a * b + c with one rounding per lane; and a * b alone, for a product that
-// feeds no packed add (see above).
+// a * b + c with one rounding per lane; and a * b alone.  Where mul2's result
+// feeds a packed add (or subtraction), there may be one rounding or two (see
+// above): a caller for whom that matters takes another way.
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));

@@ -183,9 +183,10 @@ __global__ void __launch_bounds__(RowShape<1, WARPS>::BLOCK,
   }
 }
 
-// Rows longer than registers hold: one block per row, the row read three times
-// (from L2 after the first).
-
+// Rows longer than the ring or the registers hold (float32 past 14,076 columns,
+// 16-bit past 16,384): one block per row, the row read three times (from L2 after
+// the first), one element an access.  2048 x 16384 float32: 77 us, 3.5 TB/s (2048 x
+// 12288 with the ring 41, 5.0); 4096 x 32768 bfloat16: 224 us, 2.4 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(LN_LONG_T)
     ln_forward_long(const T* __restrict__ x, int64_t ldx, int64_t rows, int cols, const T* __restrict__ w,

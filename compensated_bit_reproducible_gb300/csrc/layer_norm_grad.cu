@@ -37,6 +37,8 @@ struct Backward {
   __device__ __forceinline__ int col(int u) const { return (u * RS::T + t) * V - (MODE == ALIKE ? shift : 0); }
   __device__ __forceinline__ bool whole(int u) const { return (u + 1) * RS::T * V <= cols && (u > 0 || !shift); }
   // One pair: x and dy are zero outside the row, and with dy all its products.
+  // (g feeds sums here and in store(): with its own rounding or, contracted,
+  // without it; either is within the sums' error.)
   __device__ __forceinline__ void pair(int h, F2 x, F2 d, F2 w, F2 level, F2 width, F2& s0, F2& s1) {
     hh[h] = mul2(sub2(x, level), width);
     g[h] = mul2(d, w);
@@ -89,7 +91,7 @@ struct Backward {
 
 // x and dy side by side in a stage of the ring.
 //
-// Bound by DRAM and by the row's latency (one sum, two blocks per SM at 126
+// Bound by DRAM and by the row's latency (one sum, two blocks per SM at 125
 // registers: the columns' sums, h and g stay in registers).  32768 x 4096
 // bfloat16: 136 us, 5.9 TB/s; 4096 x 4096 float32: 44 us, 4.6 TB/s with the 10 MB
 // of partial rows written and read again, which the second kernel does in 3 us.
@@ -174,6 +176,10 @@ __global__ void __launch_bounds__(RowShape<1, WARPS>::BLOCK, RowShape<1, WARPS>:
   k.leave(part, (float*)ring_bytes);
 }
 
+// Rows longer than the ring holds (float32 past 11,260 columns, 16-bit past
+// 16,384): a block per row, read twice, its column sums in global memory, one
+// element an access.  Bound by the accesses: 2048 x 12288 float32 202 us, 1.5
+// TB/s (2048 x 8192 with the ring 43, 4.7); 4096 x 32768 bfloat16 1342 us, 0.6 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(LN_LONG_T)
     ln_backward_long(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx, int64_t rows,

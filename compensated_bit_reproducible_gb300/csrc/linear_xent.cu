@@ -15,8 +15,8 @@
 // products are scaled back.
 //
 // Bound by the tensor cores and, over milliseconds, by the power limit: loss and
-// gradient of 8192 x 32768 x 2048 bfloat16 take 2.74 ms for four products (the
-// logits twice), 1.60 PFLOP/s.  A half of the vocabulary (16384 columns): g 304
+// gradient of 8192 x 32768 x 2048 bfloat16 take 2.73 to 2.83 ms for four products
+// (the logits twice), 1.55 to 1.61 PFLOP/s.  A half of the vocabulary (16384 columns): g 304
 // us, dh 351 (256 tiles are 3.4 rounds of 76 pairs), dweight 306.
 //
 // Every tile's inner dimension is walked in order and nothing is added by
@@ -413,7 +413,9 @@ static cudaError_t pack_operand(Operand<T>& o, const T* p, int64_t ld, int64_t r
 static size_t up1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
 
 // Columns of a piece of the vocabulary in the gradient: g takes at most
-// XENT_PIECE bytes.
+// XENT_PIECE bytes.  Pieces get narrow as rows get many, and dh's float32 sums are
+// read and written once a piece: 8192 rows of 32768 x 2048 run at 1.68 PFLOP/s (6
+// n vocab cols operations), 32768 rows at 1.39, 131072 rows of 32768 x 1024 at 1.03.
 constexpr size_t XENT_PIECE = 256u << 20;
 static int64_t piece_width(int64_t n, int64_t vocab) {
   int64_t w = (int64_t)(XENT_PIECE / 2 / (size_t)n) / 256 * 256;
@@ -438,8 +440,17 @@ static int tile_cols(int64_t m, int64_t n, bool fill) {
 }
 
 // Ranges of the inner dimension: the number that costs least, in steps of a
-// tile (256 x 256 x 64, 0.27 us): rounds of tiles, each with a few steps of
-// filling, and each range's float32 sums written and read again.
+// tile (256 x 256 x 64, 0.27 us at 1.9 PFLOP/s of 76 pairs): rounds of tiles, each
+// with a few steps of filling, and each range's float32 sums written and read
+// again.  The gradient in us with one number for both its products, and by the
+// rule:
+//                                     1     2     4     8    16   rule
+//   float16   1003 x 20011 x  777   204   214   266   426   739   137
+//   bfloat16   256 x 32768 x 1024   218   294   406   388   381    85
+//               64 x 50000 x  512   291   174   115    85    72    72
+//             2048 x 32768 x 1024   340   395   542   860  1480   275
+//             8192 x  2048 x  256    85    75    73    92   142    61
+//             4096 x 32768 x 2048   953  1179  1407  1989  3293   954
 static int split_count(int64_t m, int64_t n, int tn, int64_t k, bool carried) {
   const int64_t tiles = ((m + TG_M - 1) / TG_M) * ((n + tn - 1) / tn), kb = (k + TG_K - 1) / TG_K;
   const double traffic = (double)m * n * 8 / 1.6e6;   // bytes of a step's time at 6 TB/s

@@ -21,10 +21,10 @@
 // (warps 4..7 the first half of a tile's columns, in runs of 32, 8..11 the
 // rest).
 //
-// 8192 x 32768 x 2048 bfloat16: 583 us, 1.88 PFLOP/s, in 20 calls.  In 200
-// calls back to back the loss (this kernel and the join) takes 618 to 625 us, a
-// library's product alone, which writes the logits, 581; over 3 s, under the
-// power limit, 651 and 631.  The epilogue's instructions draw on the same power.
+// 8192 x 32768 x 2048 bfloat16: 592 us, 1.86 PFLOP/s, in 20 calls.  In 200
+// calls back to back the loss (this kernel and the join) takes 629 to 636 us, a
+// library's product alone, which writes the logits, 576 to 591; over 3 s, under
+// the power limit, 656 and 633.  The epilogue's instructions draw on the same power.
 // Bands of tiles (TileWalk) took half of a weight gradient from 331 to 305 us.
 //
 // Every wait is bounded: after about two seconds it sets both words of TileError and the block

@@ -364,7 +364,12 @@ repro_status stable_linear_xent(const void* h, int64_t n, int64_t cols, int64_t 
    whose softmax gradient, 2 n bytes per column, stays within 256 MiB (at least
    256 columns), plus 4 n cols bytes where there is more than one piece.  The
    16-bit softmax gradient is held for dloss / max |dloss| (exactly 1 where
-   all are equal) times a power of two, so dloss may be of any size.  Where a product has few tiles, up to 16 float32
+   all are equal) times a power of two, so dloss may be of any size; in half its
+   elements carry an error of up to 2^-39 of the largest finite |dloss|, which
+   shows in rows whose own is below about 2^-20 of it.  An infinite or NaN dloss
+   stays in its row of dh, and reaches all of dweight.  A row of h without a label
+   enters dweight's product with zeros, so it has to be finite (a NaN in it makes
+   that column of dweight NaN).  Where a product has few tiles, up to 16 float32
    copies of its result are summed.  A label >= vocab makes its row of dh and
    all of dweight NaN.  Bits of both calls depend on values, shapes and types
    alone. */
