@@ -507,13 +507,13 @@ struct Mat {
   uintptr_t begin() const { return (uintptr_t)p; }
   uintptr_t end() const { return rows ? (uintptr_t)p + ((size_t)(rows - 1) * ld + cols) * size : (uintptr_t)p; }
 };
-// Whether two matrices share an element.  With one row stride (a single row takes
-// the other's) they may be column slices of one buffer: b's rows then start the
-// same number of bytes after a's, and lie between the end of a's row and its next.
+// Whether two matrices share a byte.  With one row stride (a single row takes the
+// other's) they may be column slices of one buffer: b's rows then start the same
+// number of bytes after a's, and lie between the end of a's row and its next.
 bool overlap(const Mat& a, const Mat& b) {
   if (!a.p || !b.p || !a.rows || !b.rows || a.begin() >= b.end() || b.begin() >= a.end()) return false;
-  const uintptr_t step = (uintptr_t)(a.rows > 1 ? a.ld : b.ld) * a.size;
-  if (a.size != b.size || (a.rows > 1 && b.rows > 1 && a.ld != b.ld)) return true;
+  const uintptr_t sa = (uintptr_t)a.ld * a.size, sb = (uintptr_t)b.ld * b.size, step = a.rows > 1 ? sa : sb;
+  if (a.rows > 1 && b.rows > 1 && sa != sb) return true;
   const uintptr_t after = b.begin() >= a.begin() ? (b.begin() - a.begin()) % step
                                                  : (step - (a.begin() - b.begin()) % step) % step;
   return after < (uintptr_t)a.cols * a.size || after + (uintptr_t)b.cols * b.size > step;

@@ -62,6 +62,7 @@ def test_shared_elements(L, call, change):
 # the same of vectors: tokens and labels (B, C, D below), weights, statistics; one element in common
 VECTORS = [
     (embedding, dict(out=at(B, 3, 8))), (embedding_grad, dict(dw=at(B, 3, 8))),
+    (layer_norm, dict(ldx=32, mean=at(A, 26))), (xent, dict(ldw=16, loss=at(B, 10))), (xent, dict(ldw=16, loss=at(B, 6))),
     (layer_norm, dict(y=at(B, 7))), (layer_norm, dict(y=at(C, 7))), (layer_norm, dict(mean=at(A, 30))),
     (layer_norm, dict(mean=at(B, 6))), (layer_norm, dict(rstd=at(C, 6))), (layer_norm, dict(rstd=A)),
     (layer_norm_grad, dict(dx=at(C, 7))), (layer_norm_grad, dict(dx=at(D, 3, 4))), (layer_norm_grad, dict(dx=E)),
@@ -80,6 +81,8 @@ def test_vectors_in_an_output(L, call, change):
 @pytest.mark.parametrize("call,change", [
     (embedding, dict(out=at(B, 4, 8))), (layer_norm, dict(y=A)), (layer_norm, dict(y=at(B, 8))), (layer_norm, dict(mean=at(A, 32))),
     (layer_norm, dict(w=None, b=None)), (layer_norm_grad, dict(dx=A)), (layer_norm_grad, dict(dw=None, db=None)),
-    (layer_norm_grad, dict(dx=at(D, 4, 4))), (xent, dict(loss=at(C, 4, 8))), (xent_grad, dict(dh=at(E, 4, 4)))])
+    (layer_norm_grad, dict(dx=at(D, 4, 4))), (xent, dict(loss=at(C, 4, 8))), (xent_grad, dict(dh=at(E, 4, 4))),
+    # between two rows of a matrix, of another type
+    (layer_norm, dict(ldx=32, mean=at(A, 8), rstd=at(A, 32 + 24))), (xent, dict(ldw=16, loss=at(B, 8)))])
 def test_vectors_beside_an_output(L, call, change):
     assert call(L, **change) == ENV
